@@ -38,12 +38,14 @@ __device__ __forceinline__ float ex2_fast(float x) {
 }
 
 // 16-byte streaming load through the non-coherent path without L1 allocation: every logit
-// is read once by the row-statistics pass.
+// is read once by the row-statistics pass.  Volatile, so that it stays behind the wait for the
+// kernel before this one (griddepcontrol.wait, volatile too) where its address is known
+// earlier: what it reads may be that kernel's output.
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {
     uint4 r;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-        : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-        : "l"(p));
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
     return r;
 }
 
