@@ -30,6 +30,11 @@ constexpr int kLinMaxSide = 1 << 30, kLinMaxK = 1 << 28;  // tile coordinates st
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// Arrays of 4-byte words (those that are not NULL).
+template <class... P>
+bool words_aligned(P... p) {
+    return (aligned_to(p, 4) && ...);
+}
 
 // Raise a kernel's limits (dynamic shared memory, clusters above eight CTAs) once per device.
 struct KernelLimits {
@@ -420,6 +425,7 @@ int spec_verify_probs(const void* target_probs, const void* draft_probs, const i
     if (!target_probs || !uniforms || !out_tokens || !out_n_accepted) return SPEC_EINVAL;
     if (gamma > 0 && !draft_tokens) return SPEC_EINVAL;
     if (!aligned16(target_probs) || !aligned16(draft_probs)) return SPEC_EINVAL;
+    if (!words_aligned(draft_tokens, uniforms, draft_lens, out_tokens, out_n_accepted, d_status)) return SPEC_EINVAL;
     int32_t* status = nullptr;
     int sm_count = 0;
     int rc = d_status ? current_sm_count(&sm_count) : library_device(&status, &sm_count);
@@ -456,7 +462,7 @@ int spec_rms_norm_fp8(const void* x, const void* residual, const void* gain, int
                       void* out_codes, float* out_scale, void* out_residual, void* stream) {
     int rc = norm_check(x, residual, gain, rows, d, eps, dtype, out_codes, out_residual);
     if (rc || rows == 0) return rc;
-    if (!out_scale || !aligned_to(out_scale, 4)) return SPEC_EINVAL;
+    if (!out_scale || !words_aligned(out_scale)) return SPEC_EINVAL;
     int sm_count = 0;
     rc = current_sm_count(&sm_count);
     if (rc) return rc;
@@ -478,6 +484,7 @@ int spec_linear(const void* x, const void* weight, const void* bias, const void*
     if (rows == 0) return SPEC_OK;
     if (!x || !weight || !out || !aligned16(x) || !aligned16(weight)) return SPEC_EINVAL;
     if (fp8 ? (!x_scale || !w_scale) : (x_scale || w_scale)) return SPEC_EINVAL;
+    if (!words_aligned(x_scale, w_scale, d_status)) return SPEC_EINVAL;
     const size_t os = out_dtype == SPEC_F32 ? 4 : 2;
     if (!aligned_to(out, os) || !aligned_to(bias, os) || !aligned_to(residual, os)) return SPEC_EINVAL;
     int32_t* status = nullptr;
