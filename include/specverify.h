@@ -435,7 +435,9 @@ int spec_rms_norm(const void *x, const void *residual, const void *gain, int row
 int spec_rms_norm_fp8(const void *x, const void *residual, const void *gain, int rows, int d, float eps, int dtype,
                       void *out_codes, float *out_scale, void *out_residual, void *stream);
 
-/* Activation of spec_linear. */
+/* Activation of spec_linear, in fp32: off by about 2^-21 of the value, and where it vanishes (v -> -inf)
+ * by 2^-21 and the rounding of its exponential's argument t, |t| 2^-22 (SILU: t = v, GELU: v^2 / 2,
+ * the tanh form: its sigmoid's argument). */
 typedef enum {
     SPEC_ACT_NONE = 0,
     SPEC_ACT_RELU = 1,
