@@ -467,6 +467,23 @@ int spec_linear(const void *x, const void *weight, const void *bias, const void 
                 const float *w_scale, int rows, int N, int K, int in_dtype, int out_dtype, int activation,
                 void *out, int32_t *d_status, void *stream);
 
+/* The kernel that spec_linear takes (spec_linear_form). */
+typedef enum {
+    SPEC_LINEAR_FEW = 0,   /* a stream of the weight, one to four tokens */
+    SPEC_LINEAR_TILES = 1, /* one CTA per tile, or `splits` CTAs that share its K */
+    SPEC_LINEAR_PAIRS = 2  /* CTA pairs */
+} spec_linear_kind;
+
+/*
+ * Diagnostic: how spec_linear would do a product of these sizes (rows >= 1), as out_form[3] = a
+ * spec_linear_kind, the tokens of a tile, and the CTAs that share a tile's K.  The choice depends on
+ * the sizes, on in_dtype, on the SMs and on how many clusters of 2, 4 and 8 CTAs the device holds at
+ * once: sm_count > 0 takes these from sm_count (at least 2) and clusters[3], without a device, and
+ * sm_count 0 from the current device, whose clusters are written to `clusters` unless it is NULL.  Host
+ * pointers; nothing is launched.
+ */
+int spec_linear_form(int rows, int N, int K, int in_dtype, int sm_count, int32_t *clusters, int32_t *out_form);
+
 /*
  * Vocabulary-parallel sampling verify ("How speculative decoding makes LLMs go brrr":
  * pseudocode and module 3, with the logits split by vocabulary column over W ranks, as a

@@ -11,7 +11,7 @@ from .specverify import (  # noqa: F401
     spec_verify_workspace_bytes, spec_row_entropy, spec_adaptive_k, spec_verify_tree, Tree,
     spec_verify_host, SPEC_FLAG_FULL_READ, SPEC_DEBUG_RACE_AGAIN, spec_lmhead_logits, spec_lmhead_row_stats,
     spec_verify_lmhead, spec_philox4x32_10, SPEC_EBADPROB, SPEC_EBADLEN, SPEC_E4M3, spec_verify_probs,
-    spec_rms_norm, spec_rms_norm_fp8, spec_linear)
+    spec_rms_norm, spec_rms_norm_fp8, spec_linear, spec_linear_form)
 from .vocab_parallel import (  # noqa: F401
     LibraryBackend, VocabShard, spec_vp_decide, spec_vp_finish, spec_vp_partials, spec_vp_race,
     verify_vocab_parallel, vocab_range)

@@ -359,55 +359,78 @@ long long resident_clusters(int size, int sm_count) {
     return known[dev][slot];
 }
 
-template <bool kFp8>
-int dispatch_linear(const void* x, const void* w, int K, LinearParams& p, int sm_count, cudaStream_t s) {
+// How a product is done: spec_linear_kind, tokens of a tile, CTAs that share a tile's K.
+struct LinearForm {
+    int kind, bn, splits;
+};
+
+int linear_kblocks(int K, bool fp8) {
+    return static_cast<int>((static_cast<long long>(K) * (fp8 ? 1 : 2) + kLinBK - 1) / kLinBK);
+}
+
+// The choice, from the sizes and the device alone.  held(size): clusters of that many CTAs that the device
+// holds at once.
+template <class Held>
+LinearForm choose_linear(bool fp8, int rows, int N, int K, int sm_count, Held held) {
     // Up to four tokens, while the channels' tiles are at most a third of the SMs, or for one token
     // and long rows three quarters (1 token, K = 4096, bf16: N = 1024 4.8 us here and 4.8 there, 4096
     // 7.6 and 9.0, 12288 17.9 and 19.1; K = 1024, e4m3: 4096 3.0 and 4.0, 8192 5.8 and 4.1, 12288 7.6
     // and 4.7; 4 tokens, K = 4096, e4m3: 8192 10.2 and 9.7; five tokens would already read twice the
     // shared memory).
-    const long long tiles128 = (p.N - 1) / kLinBM + 1;
-    const bool few = tiles128 * 3 <= sm_count || (p.rows == 1 && K * (kFp8 ? 1LL : 2LL) >= 4096 && tiles128 * 4 <= sm_count * 3LL);
-    if (p.rows <= kFewMaxRows && few && K < (1 << 20) && static_cast<uint32_t>(p.rows) * few_stride(kFp8, K) <= kFewMaxSmem)
-        return launch_linear_few<kFp8>(x, w, K, p, sm_count, s);
+    const int kblocks = linear_kblocks(K, fp8);
+    const long long n128 = (N - 1) / kLinBM + 1, n256 = (N - 1) / kPairBM + 1;
+    const bool few = n128 * 3 <= sm_count || (rows == 1 && K * (fp8 ? 1LL : 2LL) >= 4096 && n128 * 4 <= sm_count * 3LL);
+    if (rows <= kFewMaxRows && few && K < (1 << 20) && static_cast<uint32_t>(rows) * few_stride(fp8, K) <= kFewMaxSmem)
+        return LinearForm{SPEC_LINEAR_FEW, rows, 1};
     // The tile, the K split and CTA pairs or not, by an estimate of their times in ns, measured on shapes
     // of 1 to 4096 tokens x 1024 to 16384 channels x K = 1024 and 4096, bf16.  A CTA takes 118 +
     // bn / 5 ns a K slice (a pair 230 + bn / 7), whole waves of tiles; all of them together at
     // most 18 bytes a ns (KB / 18.4 a ns) from L2; the meeting of a split K 1100 + 25 bn.
     // (128 tokens, N = 1024, K = 4096: 7.7 us with 32 columns split four ways, 9.8 with 128 split
     // eight ways; 512 tokens, N = K = 4096: 17.2 us with 128 tiles of one CTA, 19.3 with 64 pairs.)
-    const long long n128 = tiles128, n256 = (p.N - 1) / kPairBM + 1;
     auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };
     long long best = -1;
-    int bn = 16, splits = 1;
-    bool pairs = false;
-    auto offer = [&](long long time, int bn_, int splits_, bool pairs_) {
+    LinearForm form{SPEC_LINEAR_TILES, 16, 1};
+    auto offer = [&](long long time, LinearForm f) {
         if (best >= 0 && time >= best) return;
         best = time;
-        bn = bn_;
-        splits = splits_;
-        pairs = pairs_;
+        form = f;
     };
     for (int b = 16; b <= 128; b *= 2) {
-        const long long tiles = ceil_div(p.rows, b) * n128;
-        const long long traffic = tiles * p.kblocks * (16 + b / 8) * 1000 / 18400;
+        const long long tiles = ceil_div(rows, b) * n128;
+        const long long traffic = tiles * kblocks * (16 + b / 8) * 1000 / 18400;
         for (int k = 1; k <= 8; k *= 2) {
-            if (k > 1 && (p.kblocks < 4 * k || tiles > resident_clusters(k, sm_count))) break;
-            const long long waves = ceil_div(tiles * k, sm_count), turns = ceil_div(p.kblocks, 2 * k);
-            offer(std::max(waves * turns * 2 * (118 + b / 5), traffic) + (k > 1 ? 1100 + 25 * b : 0), b, k, false);
+            if (k > 1 && (kblocks < 4 * k || tiles > held(k))) break;
+            const long long waves = ceil_div(tiles * k, sm_count), turns = ceil_div(kblocks, 2 * k);
+            offer(std::max(waves * turns * 2 * (118 + b / 5), traffic) + (k > 1 ? 1100 + 25 * b : 0),
+                  LinearForm{SPEC_LINEAR_TILES, b, k});
         }
     }
-    if (p.rows > 64)
+    if (rows > 64)
         for (int b = 256; b >= 64; b -= 32) {
-            const long long tiles = ceil_div(p.rows, b) * n256;
-            const long long traffic = 2 * tiles * p.kblocks * (16 + b / 16) * 1000 / 18400;
-            offer(std::max(ceil_div(tiles, sm_count / 2) * p.kblocks * (230 + b / 7), traffic), b, 1, true);
+            const long long tiles = ceil_div(rows, b) * n256;
+            const long long traffic = 2 * tiles * kblocks * (16 + b / 16) * 1000 / 18400;
+            offer(std::max(ceil_div(tiles, sm_count / 2) * kblocks * (230 + b / 7), traffic),
+                  LinearForm{SPEC_LINEAR_PAIRS, b, 1});
         }
-    if (pairs) return launch_linear_pairs<kFp8>(x, w, K, p, bn, sm_count, s);
-    if (bn == 16) return launch_linear<kFp8, 16>(x, w, K, p, splits, sm_count, s);
-    if (bn == 32) return launch_linear<kFp8, 32>(x, w, K, p, splits, sm_count, s);
-    if (bn == 64) return launch_linear<kFp8, 64>(x, w, K, p, splits, sm_count, s);
-    return launch_linear<kFp8, 128>(x, w, K, p, splits, sm_count, s);
+    return form;
+}
+
+template <bool kFp8>
+int dispatch_linear(const void* x, const void* w, int K, LinearParams& p, int sm_count, cudaStream_t s) {
+    const LinearForm f = choose_linear(kFp8, p.rows, p.N, K, sm_count, [&](int size) { return resident_clusters(size, sm_count); });
+    if (f.kind == SPEC_LINEAR_FEW) return launch_linear_few<kFp8>(x, w, K, p, sm_count, s);
+    if (f.kind == SPEC_LINEAR_PAIRS) return launch_linear_pairs<kFp8>(x, w, K, p, f.bn, sm_count, s);
+    if (f.bn == 16) return launch_linear<kFp8, 16>(x, w, K, p, f.splits, sm_count, s);
+    if (f.bn == 32) return launch_linear<kFp8, 32>(x, w, K, p, f.splits, sm_count, s);
+    if (f.bn == 64) return launch_linear<kFp8, 64>(x, w, K, p, f.splits, sm_count, s);
+    return launch_linear<kFp8, 128>(x, w, K, p, f.splits, sm_count, s);
+}
+
+bool linear_sizes_ok(int rows, int N, int K, int in_dtype) {
+    if (in_dtype != SPEC_BF16 && in_dtype != SPEC_E4M3) return false;
+    return rows >= 0 && rows <= kLinMaxSide && N >= 1 && N <= kLinMaxSide && K >= 1 && K <= kLinMaxK &&
+           K % (in_dtype == SPEC_E4M3 ? 16 : 8) == 0 && static_cast<long long>(rows) * N < (1LL << 40);
 }
 
 }  // namespace
@@ -474,13 +497,10 @@ int spec_rms_norm_fp8(const void* x, const void* residual, const void* gain, int
 int spec_linear(const void* x, const void* weight, const void* bias, const void* residual, const float* x_scale,
                 const float* w_scale, int rows, int N, int K, int in_dtype, int out_dtype, int activation, void* out,
                 int32_t* d_status, void* stream) {
-    if (in_dtype != SPEC_BF16 && in_dtype != SPEC_E4M3) return SPEC_EINVAL;
+    if (!linear_sizes_ok(rows, N, K, in_dtype)) return SPEC_EINVAL;
     if (out_dtype != SPEC_F32 && out_dtype != SPEC_BF16) return SPEC_EINVAL;
     if (activation < SPEC_ACT_NONE || activation > SPEC_ACT_SILU) return SPEC_EINVAL;
     const bool fp8 = in_dtype == SPEC_E4M3;
-    if (rows < 0 || rows > kLinMaxSide || N < 1 || N > kLinMaxSide || K < 1 || K > kLinMaxK || K % (fp8 ? 16 : 8) != 0)
-        return SPEC_EINVAL;
-    if (static_cast<long long>(rows) * N >= (1LL << 40)) return SPEC_EINVAL;
     if (rows == 0) return SPEC_OK;
     if (!x || !weight || !out || !aligned16(x) || !aligned16(weight)) return SPEC_EINVAL;
     if (fp8 ? (!x_scale || !w_scale) : (x_scale || w_scale)) return SPEC_EINVAL;
@@ -494,7 +514,7 @@ int spec_linear(const void* x, const void* weight, const void* bias, const void*
     LinearParams p{};
     p.rows = rows;
     p.N = N;
-    p.kblocks = static_cast<int>((static_cast<long long>(K) * (fp8 ? 1 : 2) + kLinBK - 1) / kLinBK);
+    p.kblocks = linear_kblocks(K, fp8);
     p.group = 16;
     p.act = activation;
     p.out_f32 = out_dtype == SPEC_F32;
@@ -507,6 +527,29 @@ int spec_linear(const void* x, const void* weight, const void* bias, const void*
     p.status = d_status ? d_status : status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return fp8 ? dispatch_linear<true>(x, weight, K, p, sm_count, s) : dispatch_linear<false>(x, weight, K, p, sm_count, s);
+}
+
+int spec_linear_form(int rows, int N, int K, int in_dtype, int sm_count, int32_t* clusters, int32_t* out_form) {
+    if (!linear_sizes_ok(rows, N, K, in_dtype) || rows < 1 || sm_count < 0 || sm_count == 1 || !out_form ||
+        (sm_count > 0 && !clusters))
+        return SPEC_EINVAL;
+    int32_t held[3];
+    if (sm_count == 0) {
+        const int rc = current_sm_count(&sm_count);
+        if (rc) return rc;
+        for (int i = 0; i < 3; ++i) {
+            held[i] = static_cast<int32_t>(resident_clusters(2 << i, sm_count));
+            if (clusters) clusters[i] = held[i];
+        }
+    } else {
+        for (int i = 0; i < 3; ++i) held[i] = clusters[i];
+    }
+    const LinearForm f = choose_linear(in_dtype == SPEC_E4M3, rows, N, K, sm_count,
+                                       [&](int size) { return static_cast<long long>(held[size == 2 ? 0 : size == 4 ? 1 : 2]); });
+    out_form[0] = f.kind;
+    out_form[1] = f.bn;
+    out_form[2] = f.splits;
+    return SPEC_OK;
 }
 
 }  // extern "C"

@@ -33,7 +33,7 @@ EXPORTED = ("spec_verify", "spec_verify_greedy", "spec_verify_ex", "spec_verify_
             "spec_lmhead_row_stats", "spec_verify_lmhead", "spec_vp_state_bytes",
             "spec_vp_partials", "spec_vp_decide", "spec_vp_race", "spec_vp_finish",
             "spec_philox4x32_10", "spec_verify_probs", "spec_rms_norm", "spec_rms_norm_fp8",
-            "spec_linear")
+            "spec_linear", "spec_linear_form")
 
 
 class SpecVerifyError(RuntimeError):
@@ -136,7 +136,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.spec_rms_norm.argtypes = [P, P, P, I, I, F, I, P, P, P]
     lib.spec_rms_norm_fp8.argtypes = [P, P, P, I, I, F, I, P, P, P, P]
     lib.spec_linear.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, P, P, P]
-    for f in ("spec_verify_probs", "spec_rms_norm", "spec_rms_norm_fp8", "spec_linear"):
+    lib.spec_linear_form.argtypes = [I, I, I, I, I, P, P]
+    for f in ("spec_verify_probs", "spec_rms_norm", "spec_rms_norm_fp8", "spec_linear", "spec_linear_form"):
         getattr(lib, f).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -560,6 +561,26 @@ def spec_linear(x, weight, bias=None, activation: str = "none", residual=None, x
     if r.__class__ is int:
         raise SpecVerifyError(r, "spec_linear")
     return r
+
+
+LINEAR_KINDS = ("few", "tiles", "pairs")  # spec_linear_kind
+
+
+def spec_linear_form(rows: int, N: int, K: int, in_dtype=torch.bfloat16, sm_count: int = 0, clusters=None):
+    """How spec_linear does a product of these sizes: (kind, tokens of a tile, CTAs that share a tile's
+    K), the kind one of LINEAR_KINDS (see ``spec_linear_form`` in the C header).  With sm_count and
+    clusters (of 2, 4 and 8 CTAs held at once) for that device, without one; else for the current."""
+    if in_dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"in_dtype must be bfloat16 or float8_e4m3fn, got {in_dtype}")
+    if (sm_count > 0) != (clusters is not None):
+        raise ValueError("sm_count and clusters go together")
+    held = (ctypes.c_int32 * 3)(*(clusters or (0, 0, 0)))
+    form = (ctypes.c_int32 * 3)()
+    rc = load_library().spec_linear_form(rows, N, K, SPEC_BF16 if in_dtype == torch.bfloat16 else SPEC_E4M3, sm_count,
+                                         held, form)
+    if rc != SPEC_OK:
+        raise SpecVerifyError(rc, "spec_linear_form")
+    return LINEAR_KINDS[form[0]], form[1], form[2]
 
 
 class Tree:
