@@ -18,7 +18,6 @@ CHECKED_LIB = os.path.join(PKG, "libspecverify_checked.so")  # SPECVERIFY_CHECKE
 SOURCES = ["specverify.cu", "operators.cu"]
 DEPS = SOURCES + ["kernels.cuh", "vocab.cuh", "device_common.cuh", "philox.cuh", "lmhead.cuh", "tensor_core.cuh",
                   "probs.cuh", "norm.cuh", "linear.cuh", "internal.h"]
-BINDING = os.path.join(PKG, "_binding.so")  # compiled argument marshalling (a Python extension)
 BINDING_DEPS = ["binding.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -41,6 +40,16 @@ def nvcc_command(out: str = LIB, extra=()) -> list:
             *extra, "-o", out, *[os.path.join(CSRC, s) for s in SOURCES]]
 
 
+def binding_path() -> str:
+    """The compiled argument marshalling (a Python extension) for the running interpreter and PyTorch,
+    whose versions are in its name: after a change of either it is built again."""
+    import sysconfig
+
+    import torch
+    tag = "".join(c if c.isalnum() else "_" for c in torch.__version__)
+    return os.path.join(PKG, f"_binding.torch_{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def binding_command() -> list:
     """g++ on the Python extension, against the running interpreter's headers and torch's."""
     import sysconfig
@@ -50,7 +59,7 @@ def binding_command() -> list:
     inc = [sysconfig.get_paths()["include"], os.path.join(t, "include"),
            os.path.join(t, "include", "torch", "csrc", "api", "include"), os.path.join(cuda_home(), "include"), INCLUDE]
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", *(f"-I{i}" for i in inc),
-            os.path.join(CSRC, "binding.cpp"), "-o", BINDING, f"-L{os.path.join(t, 'lib')}",
+            os.path.join(CSRC, "binding.cpp"), "-o", binding_path(), f"-L{os.path.join(t, 'lib')}",
             f"-Wl,-rpath,{os.path.join(t, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
@@ -62,24 +71,36 @@ def up_to_date(out: str = LIB, sources=DEPS) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def start(cmd: list, verbose: bool):
+    if verbose:
+        print(" ".join(cmd))
+    return cmd, subprocess.Popen(cmd)
+
+
 def build(force: bool = False, verbose: bool = False, extra=(), checked: bool = True) -> str:
-    """Compile libspecverify.so, the Python extension _binding.so and (unless checked=False) the
-    index-checked variant libspecverify_checked.so, side by side.  Returns the library's path."""
+    """Compile libspecverify.so, its index-checked variant libspecverify_checked.so (unless
+    checked=False) and the Python extension, side by side.  Returns the library's path.  The extension
+    also needs Python's and PyTorch's headers; where it cannot be built the library still is, for C
+    callers and the calls that go through ctypes, and a warning says so (the calls that need it raise)."""
     jobs = []
-    if force or not up_to_date(BINDING, BINDING_DEPS):
-        jobs.append(binding_command())
     if force or not up_to_date(LIB):
-        jobs.append(nvcc_command(out=LIB, extra=list(extra)))
+        jobs.append(start(nvcc_command(out=LIB, extra=list(extra)), verbose))
     if checked and (force or not up_to_date(CHECKED_LIB)):
-        jobs.append(nvcc_command(out=CHECKED_LIB, extra=["-DSPECVERIFY_CHECKED", *extra]))
-    procs = []
-    for cmd in jobs:
-        if verbose:
-            print(" ".join(cmd))
-        procs.append((cmd, subprocess.Popen(cmd)))
-    failed = [cmd for cmd, pr in procs if pr.wait() != 0]
+        jobs.append(start(nvcc_command(out=CHECKED_LIB, extra=["-DSPECVERIFY_CHECKED", *extra]), verbose))
+    missing = None
+    try:
+        if force or not up_to_date(binding_path(), BINDING_DEPS):
+            cmd, pr = start(binding_command(), verbose)
+            if pr.wait() != 0:
+                missing = f"{cmd[0]} exited with {pr.returncode}"
+    except (ImportError, OSError) as e:  # no PyTorch, no compiler
+        missing = str(e)
+    failed = [cmd for cmd, pr in jobs if pr.wait() != 0]
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
+    if missing:
+        print(f"warning: the Python extension was not built ({missing}); spec_verify_probs, spec_rms_norm, "
+              "spec_rms_norm_fp8 and spec_linear can be called from C but not from Python", file=sys.stderr)
     return LIB
 
 

@@ -8,6 +8,7 @@ is no fallback: if the compiled library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional, Sequence
 
@@ -492,15 +493,16 @@ def _operators():
     loaded library."""
     global _ops
     if _ops is None:
-        lib = load_library()
-        try:
-            from . import _binding
-        except ImportError as e:
-            raise RuntimeError("_binding.so is not built; run "
-                               "`python -m speculative_decoding_verification_31_gb300.build`") from e
-        _binding.set_library(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+        from . import build
+        lib, path = load_library(), build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; run `python -m speculative_decoding_verification_31_gb300.build`")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._binding", path)
+        binding = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(binding)
+        binding.set_library(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
             "spec_verify_probs", "spec_rms_norm", "spec_rms_norm_fp8", "spec_linear")))
-        _ops = _binding
+        _ops = binding
     return _ops
 
 
