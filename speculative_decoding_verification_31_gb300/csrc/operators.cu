@@ -137,7 +137,7 @@ struct ProbsKernel {
 template <class ET>
 int launch_probs(ProbParams& p, int sm_count, cudaStream_t s) {
     constexpr bool wide = sizeof(typename ET::storage) == 4;
-    using Two = ProbsKernel<ET, kProbChunk, wide ? 8 : 4, wide ? 2 : 3>;
+    using Two = ProbsKernel<ET, kProbChunk, wide ? 8 : 4, wide ? 2 : 3>;  // (bf16: three a SM already)
     using Three = ProbsKernel<ET, kProbChunk, 4, 3>;
     using Four = ProbsKernel<ET, kProbChunk, wide ? 4 : 2, 4>;
     // Rows of fp32 that half a chunk for every warp of 16 CTAs covers: one step of half the additions,
@@ -164,11 +164,13 @@ int launch_probs(ProbParams& p, int sm_count, cudaStream_t s) {
         cluster *= 2;
     for (; cluster > 1; cluster /= 2) {
         if (p.B <= Two::resident(cluster, sm_count)) return Two::launch(p, cluster, s);
-        if (p.B <= Three::resident(cluster, sm_count)) return Three::launch(p, cluster, s);
+        if constexpr (wide)
+            if (p.B <= Three::resident(cluster, sm_count)) return Three::launch(p, cluster, s);
         if (cluster <= 8 && p.B <= Four::resident(cluster, sm_count)) return Four::launch(p, cluster, s);
     }
     if (p.B <= Two::resident(1, sm_count)) return Two::launch(p, 1, s);
-    if (p.B <= Three::resident(1, sm_count)) return Three::launch(p, 1, s);
+    if constexpr (wide)
+        if (p.B <= Three::resident(1, sm_count)) return Three::launch(p, 1, s);
     return Four::launch(p, 1, s);
 }
 
