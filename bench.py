@@ -47,8 +47,11 @@ UNIT = "rows/s"
 # summarised in profiles/ (dram__bytes_read.sum + dram__bytes_write.sum), with the hash of
 # the code it was taken on (the element types and the row-statistics kernel with the piece
 # choice and the helpers it calls); reported as null once that code has changed.
-NCU_TRAFFIC = {"bytes": 1949927680, "sources_sha1": "26041dca03e6079a385837ca77d81ca2ff8828bc"}
-ROW_STATS_SPAN = ("inline int pick_piece_len(", "// Per-position entropies and KL divergence")
+NCU_TRAFFIC = {"bytes": 1950067968, "sources_sha1": "5697951c8b0c55d0ef1be58d5e2265b3064f19fc"}
+ROW_STATS_SOURCES = (  # file, from the first text up to the second
+    ("device_common.cuh", "// 2^x on the special-function unit", "// Two fp32 values in one register pair"),
+    ("device_common.cuh", "// Split [x0, x1) of a row", "// (value, index) argmax"),
+    ("kernels.cuh", "inline int pick_piece_len(", "// Per-position entropies and KL divergence"))
 
 
 @contextlib.contextmanager
@@ -69,15 +72,13 @@ def nvtx(name: str):
             torch.cuda.nvtx.range_pop()
 
 
-def kernel_sources_sha1() -> str:
+def kernel_sources_sha1(csrc: str = os.path.join(ROOT, "speculative_decoding_verification_31_gb300", "csrc")) -> str:
     h = hashlib.sha1()
-    csrc = os.path.join(ROOT, "speculative_decoding_verification_31_gb300", "csrc")
-    with open(os.path.join(csrc, "device_common.cuh"), "rb") as fh:
-        h.update(fh.read())
-    with open(os.path.join(csrc, "kernels.cuh"), "r") as fh:
-        text = fh.read()
-    a = text.index(ROW_STATS_SPAN[0])
-    h.update(text[a:text.index(ROW_STATS_SPAN[1], a)].encode())
+    for name, first, last in ROW_STATS_SOURCES:
+        with open(os.path.join(csrc, name), "r") as fh:
+            text = fh.read()
+        a = text.index(first)
+        h.update(text[a:text.index(last, a)].encode())
     return h.hexdigest()
 
 
