@@ -400,7 +400,7 @@ int spec_adaptive_k(const float *H_next, int B, int K, const double *centres,
  *   len_b.  The drawn token is the least x with sum_{y <= x} w(y) > u_gamma sum_y w(y), where
  *   w(y) = max(0, p_j(y) - q_j(y)) if j < len_b and w = p_j otherwise; if every residual weight
  *   is zero the draw is from p_j.  Neither row needs to sum to one.
- * The accept test is exact; sums are off by 2^-38 of W at worst.  Negative entries and NaN count as
+ * The accept test is exact; sums are off by 2^-38 of W at worst (bf16: of entries up to 2^120).  Negative entries and NaN count as
  * zero.  A last uniform <= 0 draws the first token of positive weight, one >= 1 or NaN the last.
  * out_tokens [B, gamma+1] and out_n_accepted [B] are as in spec_verify and must not overlap an
  * input.  A sequence with a draft token outside [0, V) before len_b (SPEC_EBADTOKEN), a draft
@@ -425,7 +425,8 @@ int spec_verify_probs(const void *target_probs, const void *draft_probs, const i
  * dtype.  spec_rms_norm writes n in dtype to out [rows, d] (which may be x).
  * spec_rms_norm_fp8 writes out_codes [rows, d] (e4m3, one byte each) and out_scale [rows]:
  * scale = max(max|n| / 448, 2^-126) and code = n / scale rounded to nearest, so that
- * n ~ code * scale -- the x and x_scale of spec_linear.  A row holding a NaN or an infinity
+ * n ~ code * scale -- the x and x_scale of spec_linear (a quotient within fp32's roundings, 2^-21, of
+ * the middle between two codes may become either).  A row holding a NaN or an infinity
  * becomes NaN where the formula does (in the 8-bit form the whole row and its scale).
  * Asynchronous on `stream`; no workspace.  SPEC_EINVAL for bad sizes, a negative or non-finite
  * eps, NULL or misaligned pointers.
@@ -453,7 +454,8 @@ typedef enum {
  * e.g. a draft head's residual block over the target's hidden states, or an LM head in 8 bits
  * whose logits spec_verify_ex takes.  in_dtype SPEC_BF16 (K a multiple of 8; x_scale and w_scale
  * NULL) or SPEC_E4M3 (K a multiple of 16; x_scale [rows] and w_scale [N] fp32, as
- * spec_rms_norm_fp8 writes them).  Products are summed in fp32, the epilogue is fp32 and rounds
+ * spec_rms_norm_fp8 writes them).  Products are summed in fp32 by the tensor cores (16 or 32 at a
+ * time, each addition off by up to 2^-23 of its partial sum), the epilogue is fp32 and rounds
  * once to out_dtype (SPEC_F32 or SPEC_BF16), the type of bias [N] (or NULL), residual [rows, N]
  * (or NULL) and out [rows, N]; out may be residual itself, and otherwise overlaps no input.
  * Any rows and N (at most 2^30 each, rows N < 2^40; K at most 2^28).  The result of a row does

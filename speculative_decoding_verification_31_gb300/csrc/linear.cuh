@@ -263,8 +263,8 @@ __device__ __forceinline__ void lin_finish(const LinearParams& p, float (&v)[W],
 // shared memory instead, and a lane takes four channels of W / 4 tokens: loads and stores of 8 or 16
 // bytes, and the token's scale one load instead of a shuffle a value.  (In the pair
 // kernel without a residual the turn costs more than it saves: 4096 x 16384 x 256 bf16 42 us
-// direct, 61 turned; with one, e4m3 and GELU, 172 and 139.  One CTA a tile, 1000 x 5000 x 256:
-// 11.3 and 10.0.) ----
+// direct, 61 turned; with one, e4m3 and a shorter GELU, 172 and 139 (with the present one 155 turned).
+// One CTA a tile, 1000 x 5000 x 256: 11.3 and 10.0.) ----
 
 // Four values as stored.
 template <bool kF32>

@@ -384,10 +384,12 @@ LinearForm choose_linear(bool fp8, int rows, int N, int K, int sm_count, Held he
     const bool few = n128 * 3 <= sm_count || (rows == 1 && K * (fp8 ? 1LL : 2LL) >= 4096 && n128 * 4 <= sm_count * 3LL);
     if (rows <= kFewMaxRows && few && K < (1 << 20) && static_cast<uint32_t>(rows) * few_stride(fp8, K) <= kFewMaxSmem)
         return LinearForm{SPEC_LINEAR_FEW, rows, 1};
-    // The tile, the K split and CTA pairs or not, by an estimate of their times in ns, measured on shapes
-    // of 1 to 4096 tokens x 1024 to 16384 channels x K = 1024 and 4096, bf16.  A CTA takes 118 +
-    // bn / 5 ns a K slice (a pair 230 + bn / 7), whole waves of tiles; all of them together at
-    // most 18 bytes a ns (KB / 18.4 a ns) from L2; the meeting of a split K 1100 + 25 bn.
+    // The tile, the K split and CTA pairs or not, by an estimate in ns that ranks them; its constants are
+    // fitted to shapes of 1 to 4096 tokens x 1024 to 16384 channels x K = 1024 and 4096, bf16.  A CTA takes
+    // 118 + bn / 5 ns a K slice (a pair 230 + bn / 7), whole waves of tiles; all of them together at
+    // most 18.4 KB a ns from L2; the meeting of a split K 1100 + 25 bn.  It is not the call's time: launch,
+    // set-up and the operands' way from HBM are left out (256 tokens, N = K = 4096: 9.2 us here, 17.5
+    // measured with a weight that is not in L2; 3328 tokens: 51 and 61).
     // (128 tokens, N = 1024, K = 4096: 7.7 us with 32 columns split four ways, 9.8 with 128 split
     // eight ways; 512 tokens, N = K = 4096: 17.2 us with 128 tiles of one CTA, 19.3 with 64 pairs.)
     auto ceil_div = [](long long a, long long b) { return (a + b - 1) / b; };

@@ -13,9 +13,11 @@
 // time.  Sums are pairs of fp32 (hi + lo: an exact difference p - q, compensated additions;
 // 2^-38 of the sum at worst): fp64 additions run at 1/64 of fp32's rate here, and with only the
 // reductions of lanes and chunks in fp64 the call took 65 us instead of 50 (B = 256, V = 152064,
-// fp32; 6.2 of 6.8 TB/s).  Rows of bf16 halve the bytes and not the additions, which bound them:
-// 42 us at that size with one accumulator for values in any order (43) or, as here, beginning
-// above them; 30 instead of 40 when nothing is taken from p (B = 200: 33 of 40, and 23 of 40).
+// fp32; 6.2 of 6.8 TB/s).  Rows of bf16 halve the bytes and not the time: 41 us at that size, and at
+// B = 200 33, or 24 where nothing is taken from p (floors 23, 18 and 9).  Neither memory nor a pipe is
+// full then (issue 50 %, FMA 35 %); a warp adds and reduces a chunk with no load in flight.  An
+// accumulator that begins above its bf16 values saves three of seven instructions an addition and
+// 1 us of 42.
 // Every warp stores its total into each CTA's shared memory, and after one cluster barrier each
 // CTA knows them all; the CTA whose share holds the drawn token finds its chunk from the chunk
 // sums it kept and reads that one chunk again.  No workspace, no atomics on global memory and no
