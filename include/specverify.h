@@ -455,7 +455,8 @@ typedef enum {
  * whose logits spec_verify_ex takes.  in_dtype SPEC_BF16 (K a multiple of 8; x_scale and w_scale
  * NULL) or SPEC_E4M3 (K a multiple of 16; x_scale [rows] and w_scale [N] fp32, as
  * spec_rms_norm_fp8 writes them).  Products are summed in fp32 by the tensor cores (16 or 32 at a
- * time, each addition off by up to 2^-23 of its partial sum), the epilogue is fp32 and rounds
+ * time, each addition cut off below 2^-23 of its partial sum, so bf16 sums of random signs are off by
+ * about K 2^-30 of their size in the mean), the epilogue is fp32 and rounds
  * once to out_dtype (SPEC_F32 or SPEC_BF16), the type of bias [N] (or NULL), residual [rows, N]
  * (or NULL) and out [rows, N]; out may be residual itself, and otherwise overlaps no input.
  * Any rows and N (at most 2^30 each, rows N < 2^40; K at most 2^28).  The result of a row does
