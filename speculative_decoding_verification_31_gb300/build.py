@@ -90,6 +90,8 @@ def build(force: bool = False, verbose: bool = False, extra=(), checked: bool = 
     missing = None
     try:
         if force or not up_to_date(binding_path(), BINDING_DEPS):
+            if os.path.exists(binding_path()):
+                os.remove(binding_path())  # (where the build fails, an old one is not called)
             cmd, pr = start(binding_command(), verbose)
             if pr.wait() != 0:
                 missing = f"{cmd[0]} exited with {pr.returncode}"

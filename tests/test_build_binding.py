@@ -1,5 +1,6 @@
 """The build without a GPU: the Python extension's versions are in its name, and a machine that
 cannot build it still gets the library."""
+import os
 import subprocess
 import sysconfig
 
@@ -21,9 +22,12 @@ def test_the_name_holds_both_versions(monkeypatch):
 
 @pytest.mark.parametrize("command", [["false"], ["/nonexistent/c++"]], ids=["fails", "no compiler"])
 def test_the_library_is_built_without_the_extension(sv, monkeypatch, tmp_path, capfd, command):  # noqa: F811
-    monkeypatch.setattr(build, "binding_path", lambda: str(tmp_path / "_binding.so"))
+    path = tmp_path / "_binding.so"
+    path.write_bytes(b"an old one")
+    os.utime(path, (0, 0))
+    monkeypatch.setattr(build, "binding_path", lambda: str(path))
     monkeypatch.setattr(build, "binding_command", lambda: command)
-    assert build.build() == build.LIB
+    assert build.build() == build.LIB and not path.exists()
     assert "extension was not built" in capfd.readouterr().err
 
 
